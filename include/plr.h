@@ -407,7 +407,7 @@ int plr_check(plr_layout* L, void* workspace, void* stream);
  *   - an output must not overlap an input or another output, except where a call says that
  *     it may be an input's own rows (same address and pitch);
  *   - counts of 0 rows or tokens are calls too: they write what has a value then (the
- *     gradient of weights: zeros).
+ *     gradient of weights: zeros). Arrays that have no entries then may be NULL.
  * Errors of them all: PLR_EINVAL, PLR_EALIGN, PLR_EUNSUPPORTED (a limit named below), PLR_EHIP. */
 
 /* Root-mean-square norm of a sum of contributions: for every row

@@ -89,10 +89,10 @@ extern "C" int plr_rmsnorm(int dtype, int out_dtype, int world, int64_t rows, in
   if (world > PLR_MAX_WORLD) return PLR_EUNSUPPORTED;
   if (!(eps >= 0)) return PLR_EINVAL;
   const bool f8 = out_dtype == PLR_F8;
-  if (!srcs || !gamma || (f8 && !out_scale)) return PLR_EINVAL;
+  if (!srcs || !gamma) return PLR_EINVAL;
   if (f8 && cols % 16) return PLR_EALIGN;
-  if (rows == 0) return PLR_OK;
-  if (!out) return PLR_EINVAL;
+  if (rows == 0) return PLR_OK;  // without rows no output has an entry: their addresses may be NULL
+  if (!out || (f8 && !out_scale)) return PLR_EINVAL;
   const uint64_t len = cols * elem(dtype), out_len = cols * elem(out_dtype);
   if (!a16(gamma) || !a16(residual) || !a16(sum_out) || !a16(out) || !a4(out_scale) || !a4(rstd)) return PLR_EALIGN;
   PLR_TRY(check_pitch(src_pitch, len, rows));

@@ -164,6 +164,14 @@ def test_nothing_to_do_is_no_error(plr):
     assert _call(plr, "plr_combine_backward", dict(tokens=0)) == 0
 
 
+def test_no_rows_in_8_bits_is_no_error(plr):
+    # an empty tensor's address is NULL: out_scale has no entries then
+    none = dict(rows=0, srcs=_srcs(None, None), residual=None, sum_out=None, out=None, rstd=None)
+    for out_dtype, cols, code in ((BF16, 64, 0), (F8, 64, 0), (F8, 56, ALIGN)):
+        assert _call(plr, "plr_rmsnorm", dict(none, out_dtype=out_dtype, cols=cols)) == code
+    assert _call(plr, "plr_rmsnorm", dict(rows=1, out_dtype=F8, out_scale=None)) == INVAL
+
+
 def test_workspace_sizes(plr):
     lib = plr._lib
     assert lib.plr_rmsnorm_backward_workspace_bytes(BF16, 1, 64) == 4 * 64

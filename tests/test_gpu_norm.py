@@ -170,6 +170,15 @@ def test_no_rows(plr):
     assert (dg == 0).all()
 
 
+@pytest.mark.parametrize("dt", ref.DTYPES, ids=ref.ids)
+def test_no_rows_in_8_bits(plr, dt):
+    x = torch.empty(0, 64, dtype=dt, device="cuda")
+    plr.plr_rmsnorm([x, x], torch.ones(64, dtype=dt, device="cuda"), torch.empty(0, 64, dtype=ref.F8, device="cuda"),
+                    residual=x, sum_out=torch.empty_like(x), out_scale=torch.empty(0, device="cuda"),
+                    rstd=torch.empty(0, device="cuda"))
+    torch.cuda.synchronize()
+
+
 def _backward(plr, dout, h, gamma, rstd, dsum, dx=None):
     R, C = h.shape
     dx = torch.empty(R, C, dtype=h.dtype, device="cuda") if dx is None else dx
