@@ -290,7 +290,7 @@ extern "C" int plr_group_matmul(int dtype, int out_dtype, int groups, int64_t ro
                                 size_t y_pitch, void* stream) {
   PLR_TRY(check_group(dtype, out_dtype, true, groups, rows, n, k, offsets));
   const bool f8 = dtype == PLR_F8;
-  if (f8 != (x_scale != nullptr) || f8 != (w_scale != nullptr)) return PLR_EINVAL;
+  if (f8 ? !w_scale || (!x_scale && x_rows > 0) : x_scale || w_scale) return PLR_EINVAL;
   if (x_rows < 0 || (!row_of && x_rows < rows)) return PLR_EINVAL;
   if (x_rows > kMaxRows) return PLR_EUNSUPPORTED;
   if (rows == 0) return PLR_OK;

@@ -172,6 +172,19 @@ def test_no_rows_in_8_bits_is_no_error(plr):
     assert _call(plr, "plr_rmsnorm", dict(rows=1, out_dtype=F8, out_scale=None)) == INVAL
 
 
+def test_products_of_no_rows_in_8_bits_are_no_error(plr):
+    # x_scale has no entries where x has no rows; a scale for a 16-bit type stays refused
+    none = dict(rows=0, x=None, x_rows=0, row_of=None, x_scale=None, y=None)
+    f8 = dict(none, dtype=F8, w_scale=_at(7))
+    assert _call(plr, "plr_group_matmul", none) == 0
+    assert _call(plr, "plr_group_matmul", f8) == 0
+    assert _call(plr, "plr_group_matmul", dict(f8, w_scale=None)) == INVAL
+    assert _call(plr, "plr_group_matmul", dict(f8, x=_at(1), x_rows=4)) == INVAL
+    assert _call(plr, "plr_group_matmul", dict(f8, x=_at(1), x_rows=4, x_scale=_at(6))) == 0
+    assert _call(plr, "plr_group_matmul", dict(none, x_scale=_at(6))) == INVAL
+    assert _call(plr, "plr_group_matmul", dict(none, w_scale=_at(7))) == INVAL
+
+
 def test_workspace_sizes(plr):
     lib = plr._lib
     assert lib.plr_rmsnorm_backward_workspace_bytes(BF16, 1, 64) == 4 * 64
