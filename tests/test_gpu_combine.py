@@ -135,3 +135,38 @@ def test_no_tokens(plr):
     out = torch.full((3, 64), 2.0, device="cuda")
     plr.plr_combine(torch.empty(0, 64, device="cuda"), torch.zeros(3, 2, dtype=torch.int32, device="cuda"), None, out)
     assert (out == 0).all()
+
+
+def test_more_tokens_than_workgroups(plr):
+    # some workgroups take a second token; one vector a row, so most lanes that hold a token's slots have
+    # no column of their own. Whole numbers: equal in any type
+    T, k, C = (1 << 20) + 5, 3, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randint(-3, 4, (T * k, C), generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
+    pos[torch.rand(T, k, generator=g, device="cuda") < 0.2] = -1
+    w = torch.randint(-2, 3, (T, k), generator=g, device="cuda").float()
+    kept = pos >= 0
+    rows = torch.where(kept[..., None], y[pos.clamp_min(0).long()].float(), torch.zeros(1, device="cuda"))
+    out = torch.full((T, C), 77.0, dtype=torch.bfloat16, device="cuda")
+    plr.plr_combine(y, pos, w, out)
+    assert torch.equal(out.float(), (rows * w[..., None]).sum(1))
+    dout = torch.randint(-3, 4, (T, C), generator=g, device="cuda").to(torch.bfloat16)
+    dy = torch.full((T * k, C), 77.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((T, k), 77.0, device="cuda")
+    plr.plr_combine_backward(dout, y, pos, w, dy, dw)
+    want = torch.full((T * k, C), 77.0, device="cuda")
+    want[pos[kept].long()] = (w[..., None] * dout.float()[:, None])[kept]
+    assert torch.equal(dy.float(), want)
+    assert torch.equal(dw, (rows * dout.float()[:, None]).sum(-1))
+
+
+def test_more_parts_of_rows_than_workgroups(plr):
+    # rows of two parts (128 vectors and one): 2^19 tokens at once
+    T, C = (1 << 19) + 3, 1032
+    y = torch.randint(-9, 10, (50, C), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    pos = torch.randint(-1, 50, (T, 1), generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
+    out = torch.full((T, C), 77.0, dtype=torch.bfloat16, device="cuda")
+    plr.plr_combine(y, pos, None, out)
+    want = torch.cat([y, torch.zeros_like(y[:1])])[pos[:, 0].long()]  # -1: the row of zeros
+    assert torch.equal(out, want)

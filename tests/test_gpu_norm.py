@@ -254,3 +254,40 @@ def test_on_another_stream(plr):
     plr.plr_rmsnorm([x], gamma, b, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("W", [1, 3, 8, 16])
+def test_many_long_rows(plr, W, f8):
+    # more rows than compute units and more than 128 vectors: two vectors a thread
+    dt = ref.DTYPES[W % 3]
+    srcs = [_rand(40 + w, (300, 4112), dt, 0.5) for w in range(W)]
+    res, gamma = _rand(3, (300, 4112), dt), _rand(4, (4112,), dt)
+    out_dt = ref.F8 if f8 else dt
+    _check(_run(plr, srcs, gamma, out_dt, res), ref.norm(srcs, res, gamma, EPS), dt, out_dt)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_more_rows_than_workgroups(plr, f8):
+    # 2^20 workgroups, one wave each: some take a second row; and two waves each, which share sums
+    for R, C in (((1 << 20) + 5, 16), ((1 << 20) + 3, 528)):
+        x, gamma = _rand(1, (R, 16), torch.bfloat16), _rand(2, (C,), torch.bfloat16)
+        x = x.repeat(1, C // 16)
+        out_dt = ref.F8 if f8 else torch.bfloat16
+        got = _run(plr, [x], gamma, out_dt)
+        for a in (0, R // 2, R - 4096):  # these rows in 64 bits, all rows against the first call's pieces
+            part = slice(a, a + 4096)
+            _check([t if t is None else t[part] for t in got], ref.norm([x[part]], None, gamma, EPS), torch.bfloat16, out_dt)
+        for a in range(0, R, 1 << 18):
+            part = slice(a, a + (1 << 18))
+            for t, u in zip(got, _run(plr, [x[part]], gamma, out_dt)):
+                assert t is None and u is None or torch.equal(t[part].view(torch.uint8), u.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt,C", [(torch.bfloat16, 32768), (torch.float16, 32768), (torch.float32, 16384)],
+                         ids=lambda v: ref.ids(v) if isinstance(v, torch.dtype) else str(v))
+def test_backward_of_the_longest_rows(plr, dt, C):
+    h, dout, dsum = (_rand(s, (3, C), dt) for s in (1, 2, 4))
+    gamma = _rand(3, (C,), dt)
+    rstd = torch.rsqrt(h.float().square().mean(-1) + EPS)
+    _check_backward(_backward(plr, dout, h, gamma, rstd, dsum), dout, h, gamma, rstd, dsum)

@@ -168,3 +168,23 @@ def test_gradient_against_differences(plr):
     scale = float(dw.abs().sum())
     # a softmax's third derivative is below 1: step^2, and binary32 weights over the step
     assert abs(got - float((dl.double() * u.double()).sum())) <= scale * (step ** 2 + 2.0 ** -23 / step)
+
+
+@pytest.mark.parametrize("E,k,dt", [(256, 8, torch.bfloat16), (60, 3, torch.float32)], ids=str)
+def test_more_workgroups_than_counts_kept(plr, E, k, dt):
+    # 1094 workgroups: 18 to a thread of the prefix sums, which keeps 8 counts in registers
+    x = _logits(9, 70001, E, dt)
+    x[::5] = -math.inf  # tokens without an expert
+    ids, w, pos, rt, off = _run(plr, x, k)
+    flat = torch.where(ids < 0, E, ids).reshape(-1).long()
+    n = int((flat < E).sum())
+    by = torch.argsort(flat, stable=True)
+    want = torch.full_like(by, -1)
+    want[by[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(pos.reshape(-1).long(), want)
+    assert torch.equal(rt[:n].long(), by[:n] // k) and (rt[n:] == -1).all()
+    assert off[0] == 0 and torch.equal(off[1:], torch.bincount(flat, minlength=E + 1)[:E].cumsum(0))
+    assert torch.equal(ids[::5], torch.full_like(ids[::5], -1))
+    live = torch.ones(len(x), dtype=torch.bool, device="cuda")
+    live[::5] = False
+    assert torch.equal(x[live].gather(1, ids[live].long()).float(), x[live].float().sort(-1, descending=True).values[:, :k])
