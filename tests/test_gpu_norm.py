@@ -275,7 +275,7 @@ def test_more_rows_than_workgroups(plr, f8):
         x = x.repeat(1, C // 16)
         out_dt = ref.F8 if f8 else torch.bfloat16
         got = _run(plr, [x], gamma, out_dt)
-        for a in (0, R // 2, R - 4096):  # these rows in 64 bits, all rows against the first call's pieces
+        for a in (0, R // 2, R - 4096):  # these rows in 64 bits, all rows against calls of fewer
             part = slice(a, a + 4096)
             _check([t if t is None else t[part] for t in got], ref.norm([x[part]], None, gamma, EPS), torch.bfloat16, out_dt)
         for a in range(0, R, 1 << 18):
