@@ -21,8 +21,10 @@ using atom::Elems;
 
 // Launch of a datapath kernel: `first` / `last` say whether it opens / closes the
 // call's datapath, which decides which of the thread's timing events it carries. `lds`
-// bytes of workgroup memory are reserved per workgroup beyond the kernel's own; no kernel
-// touches them: they only bound how many workgroups a compute unit holds at once.
+// bytes of workgroup memory are given per workgroup beyond the kernel's own. The datapath's
+// kernels do not touch them: there they only bound how many workgroups a compute unit holds at
+// once. The grouped products' kernels keep their tiles in them: there they are the size that the
+// kernel works with, not a choice.
 template <typename K, typename... A>
 inline void launch_dp(K kernel, dim3 grid, dim3 block, uint32_t lds, hipStream_t s, bool first, bool last,
                       A... args) {

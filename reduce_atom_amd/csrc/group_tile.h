@@ -79,7 +79,12 @@ __device__ __forceinline__ f32x16 mfma32(const Frag& c, const Frag& r, f32x16 ac
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, c.part[s]),
                                                   __builtin_bit_cast(f16x8, r.part[s]), acc, 0, 0, 0);
   else {
-    // e4m3 by e4m3, block scales of one
+    // e4m3 by e4m3, block scales of one. The instruction adds the products of 8 neighbouring
+    // elements with the bits below 2^-13 of the largest cut off (measured: a product of 4 beside
+    // one of 65536 is lost within 8 elements and kept outside), the rest in binary32: 1.5e-5 of
+    // random sums (2-norm), half a unit in the last place of bfloat16 being 3.9e-3. Accepted: the
+    // 16-bit instructions on converted operands would be exact at half the rate (8192 x 8192 x
+    // 8192: 400-427 us against 797-871).
     const i32x8 cv = {(int)c.part[0].x, (int)c.part[0].y, (int)c.part[0].z, (int)c.part[0].w,
                       (int)c.part[1].x, (int)c.part[1].y, (int)c.part[1].z, (int)c.part[1].w};
     const i32x8 rv = {(int)r.part[0].x, (int)r.part[0].y, (int)r.part[0].z, (int)r.part[0].w,

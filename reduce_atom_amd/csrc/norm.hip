@@ -2,18 +2,24 @@
 //
 // Forward, one row per workgroup at a time: h = ((x_0 + x_1) + ...) + residual in binary32 (the
 // ordered sum of plr_reduce with the residual as one more source), r = 1 / sqrt(mean(h^2) +
-// eps), y = h r gamma. Each thread keeps its vectors of h in registers, so every input
-// byte is read once and every output byte written once; the row needs one workgroup sum
-// (and one maximum more for the 8-bit output). Bound by HBM: (W + 2) e + o bytes per
-// element against about W + 5 operations. 8 x [8192, 7168] bf16 and a residual to 8-bit rows: 205
-// us (6.0 TB/s); one such row 4.7 us.
+// eps), y = h r gamma. Each thread keeps its vectors of h, so every input byte is read once and
+// every output byte written once; the row needs one workgroup sum (and one maximum more for the
+// 8-bit output). Bound by HBM: (W + 2) e + o bytes per element against about W + 5 operations. 8 x
+// [8192, 7168] bf16 and a residual to 8-bit rows: 205 us (6.0 TB/s); one such row 4.6 us.
+// Workgroups of up to 1024 threads leave 128 registers a thread. One vector a thread fits them
+// (from 9 sources on up to 4 spill), and so do two of up to 8 sources. Two vectors of 9 to 16
+// sources spill 28-44 registers into scratch (16 x [8192, 7168] bf16: 543 us, 4.1 TB/s), four of
+// 5 to 8 sources (binary32: 2 to 8) 10-34 (8 x [2048, 32768] bf16: 328 us, 4.5 TB/s; 4 sources,
+// which spill nothing: 164 us, 5.7 TB/s), four of 9 to 16 sources 108-128 (799 us, 3.2 TB/s).
 //
 // Gradient: with xh = h r and g = dy gamma,
 //   dx = r (g - xh mean(g xh)) + dsum,   dgamma = sum over rows of dy xh.
 // A workgroup walks rows b, b + B, ... and keeps its columns' dgamma sums in registers;
 // its partial sums go to the workspace and a second kernel adds the B of them in order, so
-// the result does not depend on which workgroup ends first. [8191, 7168] bf16 with dsum: 78.5 us
-// (5.9 TB/s) and 4.8 us for the second kernel.
+// the result does not depend on which workgroup ends first. [8191, 7168] bf16 with dsum: 79 us
+// (5.9 TB/s) and 4.9 us for the second kernel. Rows of more than 2048 vectors (four a thread) spill
+// 73 registers in bf16, 106 in fp16 and 5 in binary32: [2048, 32768] 266 and 315 us (2.0 and 1.7
+// TB/s), [2048, 16384] binary32 110 us (4.9 TB/s).
 #include <algorithm>
 
 #include "device_common.h"
