@@ -137,22 +137,24 @@ def test_no_tokens(plr):
     assert (out == 0).all()
 
 
-def test_more_tokens_than_workgroups(plr):
-    # some workgroups take a second token; one vector a row, so most lanes that hold a token's slots have
-    # no column of their own. Whole numbers: equal in any type
-    T, k, C = (1 << 20) + 5, 3, 8
+@pytest.mark.parametrize("k,dt", [(2, torch.float32), (3, torch.bfloat16), (5, torch.float16), (9, torch.bfloat16)],
+                         ids=str)
+def test_more_tokens_than_workgroups(plr, k, dt):
+    # some workgroups take a second token; one vector a row, so that the lanes that hold a token's slots
+    # have, but for the first, no column of their own. Whole numbers: equal in any type
+    T, C = (1 << 20) + 5, 16 // dt.itemsize
     g = torch.Generator(device="cuda").manual_seed(1)
-    y = torch.randint(-3, 4, (T * k, C), generator=g, device="cuda").to(torch.bfloat16)
+    y = torch.randint(-3, 4, (T * k, C), generator=g, device="cuda").to(dt)
     pos = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
     pos[torch.rand(T, k, generator=g, device="cuda") < 0.2] = -1
     w = torch.randint(-2, 3, (T, k), generator=g, device="cuda").float()
     kept = pos >= 0
     rows = torch.where(kept[..., None], y[pos.clamp_min(0).long()].float(), torch.zeros(1, device="cuda"))
-    out = torch.full((T, C), 77.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T, C), 77.0, dtype=dt, device="cuda")
     plr.plr_combine(y, pos, w, out)
     assert torch.equal(out.float(), (rows * w[..., None]).sum(1))
-    dout = torch.randint(-3, 4, (T, C), generator=g, device="cuda").to(torch.bfloat16)
-    dy = torch.full((T * k, C), 77.0, dtype=torch.bfloat16, device="cuda")
+    dout = torch.randint(-3, 4, (T, C), generator=g, device="cuda").to(dt)
+    dy = torch.full((T * k, C), 77.0, dtype=dt, device="cuda")
     dw = torch.full((T, k), 77.0, device="cuda")
     plr.plr_combine_backward(dout, y, pos, w, dy, dw)
     want = torch.full((T * k, C), 77.0, device="cuda")
